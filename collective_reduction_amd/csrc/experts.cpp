@@ -439,8 +439,9 @@ ccl_sim_result_t ccl_sim_expert_matmul_grad(const ccl_sim_expert_shape_t* shape,
   rc = bind(arrays, 8, s.nranks, lay, workspace, workspace_bytes, c.stream);
   if (rc != CCL_SIM_SUCCESS) return rc;
   c.scratch = static_cast<char*>(workspace) + lay.own;
-  c.rows16 = c.want_weights && starts16(rows, s.nranks);
-  c.weights16 = c.want_rows && starts16(weights, s.nranks);
+  // an array without elements may be NULL
+  c.rows16 = c.want_weights && narrow > 0 && starts16(rows, s.nranks);
+  c.weights16 = c.want_rows && matrices > 0 && starts16(weights, s.nranks);
   c.grads16 = wide > 0 && starts16(grads, s.nranks);
   const hipError_t e = device_cus(&c.num_cus);
   if (e != hipSuccess) return fail(CCL_SIM_HIP_ERROR, "device query failed: %s", hipGetErrorString(e));

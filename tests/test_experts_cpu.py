@@ -3,6 +3,9 @@
 and the oracle against brute force, autograd and differences."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -187,6 +190,31 @@ def test_empty_calls_succeed_with_null_pointers(cs):
         call(cs, "matmul", shape=sizes, rows=nobody, weights=nobody, out=nobody, offsets=nobody, bias=nobody,
              residual=nobody, preact=nobody)
     call(cs, "matmul_grad", grad_rows=None, grad_weights=None, grad_bias=None)
+
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.mark.parametrize("empty,absent,asked", [
+    ("capacity", ("rows", "grads", "preact"), "grad_weights"), ("capacity", ("rows", "grads", "weights"), "grad_bias"),
+    ("features", ("weights", "grads", "preact"), "grad_rows")])
+def test_gradients_of_nothing_read_no_array_that_is_null(empty, absent, asked):
+    """Arrays of no elements may be NULL: the call gets as far as a machine
+    without a GPU lets it.  In a process of its own, with no GPU to be seen."""
+    code = f"""
+import test_experts_cpu as t
+from collective_reduction_amd import ccl_sim as cs
+outputs = {{k: None for k in ("grad_rows", "grad_weights", "grad_bias") if k != {asked!r}}}
+try:
+    t.call(cs, "matmul_grad", shape={{{empty!r}: 0}}, **{{k: None for k in {absent!r}}}, **outputs)
+except cs.CclSimError as e:
+    assert e.code == cs.HIP_ERROR, e
+print("returned")
+"""
+    paths = os.pathsep.join((ROOT, os.path.join(ROOT, "tests")))
+    env = {**os.environ, "HIP_VISIBLE_DEVICES": "-1", "PYTHONPATH": paths}
+    done = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and done.stdout.strip().endswith("returned"), (done.returncode, done.stderr[-500:])
 
 
 def test_binding_checks_tensors(cs):

@@ -378,6 +378,24 @@ def test_rows_far_behind_32_bits(cs):
     U.check(grad_w, value, U.sum_bound(size, used, "bfloat16", value), "grad_weights")
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_gradients_of_nothing_are_zeros(cs, dtype):
+    """No rows, or no features: zeros, and arrays without elements may be left out."""
+    t = U.TORCH[dtype]
+    shape = cs.ExpertShape(nranks=2, experts=4, capacity=0, hidden=24, features=40)
+    grad_w, grad_b = (torch.full(s, 7.0, dtype=t, device="cuda") for s in ((2, 2, 40, 24), (2, 2, 40)))
+    offsets = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    cs.ccl_sim_expert_matmul_grad(shape, None, offsets=offsets, activation="silu", grad_weights=grad_w, grad_bias=grad_b,
+                                  workspace=cs.ExpertWorkspace("matmul_grad", shape, dtype), dtype=dtype)
+    assert bool((grad_w == 0).all()) and bool((grad_b == 0).all())
+    shape = cs.ExpertShape(nranks=2, experts=4, capacity=9, hidden=24, features=0)
+    offsets = torch.tensor([[0, 4, 9], [0, 0, 5]], dtype=torch.int32, device="cuda")
+    grad_rows = torch.full((2, 9, 24), 7.0, dtype=t, device="cuda")
+    cs.ccl_sim_expert_matmul_grad(shape, None, offsets=offsets, activation="silu", grad_rows=grad_rows,
+                                  workspace=cs.ExpertWorkspace("matmul_grad", shape, dtype), dtype=dtype)
+    assert bool((grad_rows[0] == 0).all()) and bool((grad_rows[1, :5] == 0).all()) and bool((grad_rows[1, 5:] == 7).all())
+
+
 def test_bad_offsets_stay_inside_the_buffers(cs):
     """Offsets that lead outside or backwards are cut; the rows before the
     first bad one are still right."""
