@@ -106,7 +106,13 @@ struct Array {
   bool output;
   int same_as;       // an output that may be this input's buffers, else -1
   RankPtrs* to;      // where the kernels' copy goes
+  bool used = true;  // the call has it: its kernels ask for its addresses, also where it has no elements
+
+  bool touched() const { return used && bytes > 0; }
 };
+
+// The addresses of arrays without elements.
+const void* const kNowhere[CCL_SIM_MAX_RANKS] = {};
 
 struct Span {
   uintptr_t lo, hi;
@@ -120,7 +126,7 @@ ccl_sim_result_t check_overlap(const Array* arrays, int count, int nranks, uintp
   Span outs[3 * CCL_SIM_MAX_RANKS];
   int n = 0;
   for (int i = 0; i < count; ++i)
-    if (arrays[i].output && arrays[i].bytes > 0)
+    if (arrays[i].output && arrays[i].touched())
       for (int r = 0; r < nranks; ++r) {
         const uintptr_t p = reinterpret_cast<uintptr_t>(arrays[i].ptrs[r]);
         outs[n++] = Span{p, p + arrays[i].bytes, r, i};
@@ -134,7 +140,7 @@ ccl_sim_result_t check_overlap(const Array* arrays, int count, int nranks, uintp
     return std::upper_bound(outs, outs + n, lo, [](uintptr_t v, const Span& s) { return v < s.hi; });
   };
   for (int i = 0; i < count; ++i) {
-    if (arrays[i].bytes == 0) continue;
+    if (!arrays[i].touched()) continue;
     for (int r = 0; r < nranks; ++r) {
       const uintptr_t lo = reinterpret_cast<uintptr_t>(arrays[i].ptrs[r]), hi = lo + arrays[i].bytes;
       if (ws < hi && lo < ws_end)
@@ -154,7 +160,7 @@ ccl_sim_result_t check_overlap(const Array* arrays, int count, int nranks, uintp
 ccl_sim_result_t bind(const Array* arrays, int count, int nranks, const Layout& lay, void* workspace,
                       size_t workspace_bytes, hipStream_t stream) {
   for (int i = 0; i < count; ++i) {
-    if (arrays[i].bytes == 0) continue;  // nothing of it is touched
+    if (!arrays[i].touched()) continue;
     const ccl_sim_result_t rc = check_ptrs(arrays[i].ptrs, nranks, arrays[i].name, arrays[i].align);
     if (rc != CCL_SIM_SUCCESS) return rc;
   }
@@ -168,12 +174,13 @@ ccl_sim_result_t bind(const Array* arrays, int count, int nranks, const Layout& 
   const ccl_sim_result_t rc = check_overlap(arrays, count, nranks, ws, ws + lay.total);
   if (rc != CCL_SIM_SUCCESS) return rc;
   for (int i = 0; i < count; ++i) {
-    if (arrays[i].bytes == 0) continue;
+    if (!arrays[i].used) continue;
+    const Arrays ptrs = arrays[i].bytes > 0 ? arrays[i].ptrs : kNowhere;
     if (nranks <= kInlineRanks) {
-      for (int r = 0; r < nranks; ++r) arrays[i].to->p[r] = arrays[i].ptrs[r];
+      for (int r = 0; r < nranks; ++r) arrays[i].to->p[r] = ptrs[r];
     } else {
       const void** table = reinterpret_cast<const void**>(static_cast<char*>(workspace) + size_t(i) * lay.table_bytes);
-      const hipError_t e = upload_table(table, arrays[i].ptrs, nranks, stream);
+      const hipError_t e = upload_table(table, ptrs, nranks, stream);
       if (e != hipSuccess) return fail(CCL_SIM_HIP_ERROR, "pointer table upload failed: %s", hipGetErrorString(e));
       arrays[i].to->table = reinterpret_cast<const uint64_t*>(table);
     }
@@ -322,8 +329,8 @@ ccl_sim_result_t ccl_sim_expert_combine(const ccl_sim_expert_shape_t* shape, con
   const Array arrays[] = {
       {"sendbufs", sendbufs, s.capacity * s.hidden * es, es, false, -1, &c.rows},
       {"places", reinterpret_cast<Arrays>(places), choices * 4, 4, false, -1, &c.places},
-      {"weights", reinterpret_cast<Arrays>(weights), c.has_weights ? choices * 4 : 0, 4, false, -1, &c.weights},
-      {"residual", residual, c.has_residual ? tokens : 0, es, false, -1, &c.residual},
+      {"weights", reinterpret_cast<Arrays>(weights), choices * 4, 4, false, -1, &c.weights, c.has_weights},
+      {"residual", residual, tokens, es, false, -1, &c.residual, c.has_residual},
       {"recvbufs", as_in(recvbufs), tokens, es, true, 3, &c.out},
   };
   rc = bind(arrays, 5, s.nranks, layout(CCL_SIM_EXPERT_COMBINE, s, dtype), workspace, workspace_bytes, c.stream);
@@ -351,12 +358,12 @@ ccl_sim_result_t ccl_sim_expert_combine_grad(const ccl_sim_expert_shape_t* shape
   const uint64_t choices = s.tokens * uint64_t(s.topk), rows = s.capacity * s.hidden * es;
   const Array arrays[] = {
       {"grads", grads, s.tokens * s.hidden * es, es, false, -1, &c.in},
-      {"sendbufs", sendbufs, c.has_grad_weights ? rows : 0, es, false, -1, &c.rows},
+      {"sendbufs", sendbufs, rows, es, false, -1, &c.rows, c.has_grad_weights},
       {"places", reinterpret_cast<Arrays>(places), choices * 4, 4, false, -1, &c.places},
-      {"weights", reinterpret_cast<Arrays>(weights), c.has_weights ? choices * 4 : 0, 4, false, -1, &c.weights},
-      {"grad_rows", as_in(grad_rows), c.has_grad_rows ? rows : 0, es, true, -1, &c.grad_rows},
-      {"grad_weights", reinterpret_cast<Arrays>(grad_weights), c.has_grad_weights ? choices * 4 : 0, 4, true, -1,
-       &c.grad_weights},
+      {"weights", reinterpret_cast<Arrays>(weights), choices * 4, 4, false, -1, &c.weights, c.has_weights},
+      {"grad_rows", as_in(grad_rows), rows, es, true, -1, &c.grad_rows, c.has_grad_rows},
+      {"grad_weights", reinterpret_cast<Arrays>(grad_weights), choices * 4, 4, true, -1, &c.grad_weights,
+       c.has_grad_weights},
   };
   rc = bind(arrays, 6, s.nranks, layout(CCL_SIM_EXPERT_COMBINE_GRAD, s, dtype), workspace, workspace_bytes, c.stream);
   if (rc != CCL_SIM_SUCCESS) return rc;
@@ -384,11 +391,11 @@ ccl_sim_result_t ccl_sim_expert_matmul(const ccl_sim_expert_shape_t* shape, cons
   c.has_preact = preact != nullptr;
   const Array arrays[] = {
       {"rows", rows, s.capacity * s.hidden * es, es, false, -1, &c.rows},
-      {"offsets", reinterpret_cast<Arrays>(offsets), c.has_offsets ? (per_rank + 1) * 4 : 0, 4, false, -1, &c.offsets},
+      {"offsets", reinterpret_cast<Arrays>(offsets), (per_rank + 1) * 4, 4, false, -1, &c.offsets, c.has_offsets},
       {"weights", weights, per_rank * s.features * s.hidden * es, es, false, -1, &c.weights},
-      {"bias", bias, c.has_bias ? per_rank * s.features * es : 0, es, false, -1, &c.bias},
-      {"residual", residual, c.has_residual ? outs : 0, es, false, -1, &c.residual},
-      {"preact", as_in(preact), c.has_preact ? outs : 0, es, true, -1, &c.preact},
+      {"bias", bias, per_rank * s.features * es, es, false, -1, &c.bias, c.has_bias},
+      {"residual", residual, outs, es, false, -1, &c.residual, c.has_residual},
+      {"preact", as_in(preact), outs, es, true, -1, &c.preact, c.has_preact},
       {"out", as_in(out), outs, es, true, 4, &c.out},
   };
   const Layout lay = layout(CCL_SIM_EXPERT_MATMUL, s, dtype);
@@ -427,13 +434,13 @@ ccl_sim_result_t ccl_sim_expert_matmul_grad(const ccl_sim_expert_shape_t* shape,
   const uint64_t matrices = per_rank * s.features * s.hidden * es;
   const Array arrays[] = {
       {"grads", grads, wide, es, false, -1, &c.grads},
-      {"rows", rows, c.want_weights ? narrow : 0, es, false, -1, &c.rows},
-      {"offsets", reinterpret_cast<Arrays>(offsets), c.has_offsets ? (per_rank + 1) * 4 : 0, 4, false, -1, &c.offsets},
-      {"weights", weights, c.want_rows ? matrices : 0, es, false, -1, &c.weights},
-      {"preact", preact, c.has_preact ? wide : 0, es, false, -1, &c.preact},
-      {"grad_rows", as_in(grad_rows), c.want_rows ? narrow : 0, es, true, -1, &c.grad_rows},
-      {"grad_weights", as_in(grad_weights), c.want_weights ? matrices : 0, es, true, -1, &c.grad_weights},
-      {"grad_bias", as_in(grad_bias), c.want_bias ? per_rank * s.features * es : 0, es, true, -1, &c.grad_bias},
+      {"rows", rows, narrow, es, false, -1, &c.rows, c.want_weights},
+      {"offsets", reinterpret_cast<Arrays>(offsets), (per_rank + 1) * 4, 4, false, -1, &c.offsets, c.has_offsets},
+      {"weights", weights, matrices, es, false, -1, &c.weights, c.want_rows},
+      {"preact", preact, wide, es, false, -1, &c.preact, c.has_preact},
+      {"grad_rows", as_in(grad_rows), narrow, es, true, -1, &c.grad_rows, c.want_rows},
+      {"grad_weights", as_in(grad_weights), matrices, es, true, -1, &c.grad_weights, c.want_weights},
+      {"grad_bias", as_in(grad_bias), per_rank * s.features * es, es, true, -1, &c.grad_bias, c.want_bias},
   };
   const Layout lay = layout(CCL_SIM_EXPERT_MATMUL_GRAD, s, dtype);
   rc = bind(arrays, 8, s.nranks, lay, workspace, workspace_bytes, c.stream);

@@ -396,6 +396,30 @@ def test_gradients_of_nothing_are_zeros(cs, dtype):
     assert bool((grad_rows[0] == 0).all()) and bool((grad_rows[1, :5] == 0).all()) and bool((grad_rows[1, 5:] == 7).all())
 
 
+def test_more_ranks_than_inline_pointers_and_arrays_without_elements(cs):
+    """Past 64 ranks the kernels read addresses from tables, also those of
+    arrays that have no elements."""
+    n = 130
+    shape = shape_of(cs, n, 3, 4, 5, 0)
+    grad_weights, nothing = torch.full((n, 4, 3), 7.0, device="cuda"), torch.empty(n, 5, 0, device="cuda")
+    places = torch.arange(n * 12, dtype=torch.int32, device="cuda").view(n, 4, 3) % (n * 5)
+    cs.ccl_sim_expert_combine_grad(shape, nothing[:, :4].contiguous(), places, sendbufs=nothing, grad_rows=nothing.clone(),
+                                   grad_weights=grad_weights, workspace=cs.ExpertWorkspace("combine_grad", shape))
+    assert bool((grad_weights == 0).all())
+    offsets = torch.zeros(n, 3, dtype=torch.int32, device="cuda")
+    shape = cs.ExpertShape(nranks=n, experts=2 * n, capacity=0, hidden=12, features=20)
+    grad_w, grad_b = torch.full((n, 2, 20, 12), 7.0, device="cuda"), torch.full((n, 2, 20), 7.0, device="cuda")
+    cs.ccl_sim_expert_matmul_grad(shape, None, offsets=offsets, activation="gelu", grad_weights=grad_w, grad_bias=grad_b,
+                                  workspace=cs.ExpertWorkspace("matmul_grad", shape), dtype="float32")
+    assert bool((grad_w == 0).all()) and bool((grad_b == 0).all())
+    shape = cs.ExpertShape(nranks=n, experts=2 * n, capacity=6, hidden=12, features=0)
+    offsets[:, 1], offsets[:, 2] = 2, 5
+    grad_rows = torch.full((n, 6, 12), 7.0, device="cuda")
+    cs.ccl_sim_expert_matmul_grad(shape, None, offsets=offsets, activation="gelu", grad_rows=grad_rows,
+                                  workspace=cs.ExpertWorkspace("matmul_grad", shape), dtype="float32")
+    assert bool((grad_rows[:, :5] == 0).all()) and bool((grad_rows[:, 5:] == 7).all())
+
+
 def test_bad_offsets_stay_inside_the_buffers(cs):
     """Offsets that lead outside or backwards are cut; the rows before the
     first bad one are still right."""
