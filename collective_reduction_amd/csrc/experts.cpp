@@ -49,8 +49,10 @@ ccl_sim_result_t check_shape(int op, const Shape* s) {
     if (s->features > kMaxWidth)
       return fail(CCL_SIM_INVALID_ARGUMENT, "features=%zu is above %zu", s->features, kMaxWidth);
     if (s->hidden == 0) return fail(CCL_SIM_INVALID_ARGUMENT, "a product over hidden=0 elements");
-    // a launch holds fewer than 2^32 threads, 256 to a tile of 128 x 128 or
-    // to 64 columns of an expert
+    // a launch holds fewer than 2^32 threads: 256 to 64 rows or more and 128
+    // columns or more (the pass over the activation's gradient), 256 to 64
+    // columns of an expert (few rows).  The tile kernel's workgroups take
+    // turns; its tiles are counted in 32 bits.
     const uint64_t per_rank = uint64_t(s->experts / s->nranks), f = s->features / 128 + 1, h = s->hidden / 128 + 1;
     const uint64_t tiles = std::max({n * (s->capacity / 64 + per_rank) * std::max(f, h), uint64_t(s->experts) * f * h,
                                      uint64_t(s->experts) * (s->features / 64 + 1)});

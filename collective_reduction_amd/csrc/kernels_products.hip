@@ -537,7 +537,8 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void product_kernel(ProductArgs a
   //              the offsets; a run per XCD, its workgroups taking turns.
   //   weights' gradient: every XCD takes an eighth of each expert's tiles (an
   //              expert's tiles all have its k, and experts differ in it),
-  //              one workgroup a tile.
+  //              one workgroup a tile, or taking turns where a launch cannot
+  //              hold as many.
   constexpr uint32_t kGroup = 4;
   const uint32_t xcd = blockIdx.x & 7, turn = blockIdx.x >> 3;
   const uint32_t lda = a.lda, ldb = a.ldb;
@@ -571,8 +572,9 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void product_kernel(ProductArgs a
     unit = uint32_t(total * xcd / 8) + turn;
     unit_end = uint32_t(total * (xcd + 1) / 8);
   } else {
+    const uint32_t tiles = (a.m + BM - 1) / BM * a.ntiles;
     unit = turn;
-    unit_end = turn + 1;
+    unit_end = a.nranks * a.per_rank * a.splits * ((tiles + 7) / 8);
   }
 
   // One tile.  m and k count from the expert's first row where they are its
@@ -607,9 +609,14 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void product_kernel(ProductArgs a
     } else {
       mtiles = (a.m + BM - 1) / BM;
       const uint32_t tiles = mtiles * a.ntiles, slots = (tiles + 7) / 8;
-      const uint32_t q = unit / slots, part = (xcd + q) & 7;
-      rest = tiles * part / 8 + (unit - q * slots);
-      if (q >= a.nranks * a.per_rank * a.splits || rest >= tiles * (part + 1) / 8) return j;
+      uint32_t q;
+      for (;; unit += gridDim.x >> 3) {  // over the slots that an eighth of few tiles leaves empty
+        if (unit >= unit_end) return j;
+        q = unit / slots;
+        const uint32_t part = (xcd + q) & 7;
+        rest = tiles * part / 8 + (unit - q * slots);
+        if (rest < tiles * (part + 1) / 8) break;
+      }
       j.split = q % a.splits;
       j.rank = q / a.splits / a.per_rank;
       j.expert = q / a.splits - j.rank * a.per_rank;
@@ -1198,6 +1205,9 @@ struct Operand {
   uint32_t ld = 0;
 };
 
+// A launch holds fewer than 2^32 threads, of which a workgroup has up to 512.
+constexpr uint64_t kMostBlocks = uint64_t(1) << 22;
+
 template <class T, int MODE>
 hipError_t launch_product(ProductArgs a, const Operand& x, const Operand& y, hipStream_t stream, int num_cus) {
   using S = typename T::S;
@@ -1219,6 +1229,7 @@ hipError_t launch_product(ProductArgs a, const Operand& x, const Operand& y, hip
     if (MODE == kGradWeights) {
       const uint64_t tiles = uint64_t((a.m + bm - 1) / bm) * a.ntiles;
       grid = uint64_t(a.nranks) * a.per_rank * a.splits * ((tiles + 7) / 8) * 8;
+      if (grid > kMostBlocks) grid = kMostBlocks;
     } else {
       // as many workgroups as run at once, or as there may be tiles
       const uint64_t mtiles = a.has_offsets ? a.capacity / bm + a.per_rank : (a.capacity + bm - 1) / bm;

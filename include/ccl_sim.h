@@ -509,7 +509,12 @@ int ccl_sim_persistent_ordering(ccl_sim_coll_t coll, int nranks, size_t count);
  *
  * Limits (CCL_SIM_INVALID_ARGUMENT): experts a positive multiple of nranks,
  * at most CCL_SIM_MAX_EXPERTS; topk 1 to CCL_SIM_MAX_TOPK; nranks·capacity
- * and nranks·tokens·topk below 2^31; hidden and features at most 2^20.
+ * and nranks·tokens·topk below 2^31; hidden and features at most 2^20.  In
+ * whole numbers, for dispatch, combine and its gradient
+ * nranks·tokens·(hidden / 128 + 1) below 2^31, and for the products, with
+ * H = hidden / 128 + 1 and F = features / 128 + 1, each of
+ * (nranks·(capacity / 64) + experts)·max(F, H), experts·F·H and
+ * experts·(features / 64 + 1) below 2^24.
  */
 #define CCL_SIM_MAX_EXPERTS 2048
 #define CCL_SIM_MAX_TOPK 64

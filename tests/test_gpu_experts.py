@@ -420,6 +420,37 @@ def test_more_ranks_than_inline_pointers_and_arrays_without_elements(cs):
     assert bool((grad_rows[:, :5] == 0).all()) and bool((grad_rows[:, 5:] == 7).all())
 
 
+@pytest.mark.parametrize("n,experts,hidden,features,dtype", [
+    (1, 1000, 1, 1 << 20, "bfloat16"),  # 16,384,000 tiles of 64 x 128, 512 threads each
+    (8, 2048, 600001, 1, "bfloat16"),   # 9,601,024
+    (1, 1024, 1 << 20, 4, "float32"),   # 16,777,216 tiles of 64 x 64, 256 threads each
+])
+def test_more_tiles_of_weights_than_one_launch_holds(cs, n, experts, hidden, features, dtype):
+    """Above 2^32 threads the workgroups take turns.  Small whole numbers:
+    every sum is exact, in bf16 too (at most 20 rows of products up to 4)."""
+    per_rank, capacity, t = experts // n, 64, U.TORCH[dtype]
+    rng = np.random.default_rng([23, experts])
+    counts = np.zeros((n, per_rank), np.int64)
+    for r in range(n):
+        counts[r, [0, per_rank // 3, per_rank - 1]] = 20, 1, 13
+    off = np.concatenate([np.zeros((n, 1), np.int64), np.cumsum(counts, 1)], 1).astype(np.int32)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    g = torch.randint(-2, 3, (n, capacity, features), device="cuda", generator=gen).to(t)
+    x = torch.randint(-2, 3, (n, capacity, hidden), device="cuda", generator=gen).to(t)
+    grad_w = torch.full((n, per_rank, features, hidden), 7.0, dtype=t, device="cuda")
+    shape = cs.ExpertShape(nranks=n, experts=experts, capacity=capacity, hidden=hidden, features=features)
+    cs.ccl_sim_expert_matmul_grad(shape, g, rows=x, offsets=dev(off), grad_weights=grad_w,
+                                  workspace=cs.ExpertWorkspace("matmul_grad", shape, dtype))
+    for r in range(n):
+        for e in np.nonzero(counts[r])[0]:
+            want = torch.zeros(features, hidden, device="cuda")
+            for s in range(off[r, e], off[r, e + 1]):
+                want += g[r, s].float()[:, None] * x[r, s].float()[None, :]
+            assert torch.equal(grad_w[r, e].float(), want), (r, e)
+            grad_w[r, e].zero_()
+    assert not bool(grad_w.any())
+
+
 def test_bad_offsets_stay_inside_the_buffers(cs):
     """Offsets that lead outside or backwards are cut; the rows before the
     first bad one are still right."""
