@@ -540,7 +540,7 @@ typedef enum {
 
 /* Activations of the products, with z the product plus bias:
  * NONE z; RELU max(z, 0); GELU z·Φ(z), Φ the normal distribution's function
- * (by erf); SILU z / (1 + e^-z). */
+ * (exact, not the tanh form); SILU z / (1 + e^-z). */
 typedef enum {
   CCL_SIM_ACT_NONE = 0,
   CCL_SIM_ACT_RELU = 1,

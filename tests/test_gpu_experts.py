@@ -344,6 +344,38 @@ def test_a_row_that_is_no_number_stays_alone(cs, dtype):
     U.check(out[:, rest], want[:, rest], U.sum_bound(size, 192, dtype, want)[:, rest], "the other rows")
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_gelu_far_on_the_negative_side(cs, dtype):
+    """GELU and its derivative, alone: products of one element by 1.
+
+    The normal distribution's function Φ(z) = erfc(-z / √2) / 2.  float32: the
+    argument is off by two half steps, which erfc passes on at most z² + 1
+    times (erfc(x) >= 2 / √π·e^(-x²) / (x + √(x² + 2))), erfc itself by 16
+    steps, the product with z by half a one.  bf16: e^(-x²) passes on the seven
+    half steps of its exponent z² / 2 times, the polynomial is off by 6e-7, and
+    some 20 operations by a step at most.  The density in the derivative: the
+    exponent's three half steps, z² / 2 times, and some 8 more."""
+    from scipy.special import erfc
+    z = torch.linspace(-12, 6, 4001).to(U.TORCH[dtype])
+    z64, n = z.double().numpy(), len(z)
+    half = 2.0 ** -24
+    phi = {"float32": half * (2 * (z64 ** 2 + 1) + 33), "bfloat16": 6e-7 + half * (3.5 * z64 ** 2 + 40)}[dtype]
+    normal, density = 0.5 * erfc(-z64 / np.sqrt(2)), np.exp(-z64 ** 2 / 2) / np.sqrt(2 * np.pi)
+    shape = cs.ExpertShape(nranks=1, experts=1, capacity=n, hidden=1, features=1)
+    one, out = torch.ones(1, 1, 1, 1, dtype=U.TORCH[dtype], device="cuda"), torch.empty(1, n, 1, dtype=U.TORCH[dtype], device="cuda")
+    cs.ccl_sim_expert_matmul(shape, dev(z).view(1, n, 1), one, out, activation="gelu")
+    want = z64 * normal
+    error = np.abs(want) * (phi + half)
+    U.check(out.view(n), want, error + U.HALF[dtype] * (np.abs(want) + error), "gelu")
+    grad = torch.empty_like(out)
+    cs.ccl_sim_expert_matmul_grad(shape, torch.ones_like(out), weights=one, preact=dev(z).view(1, n, 1), activation="gelu",
+                                  grad_rows=grad, workspace=cs.ExpertWorkspace("matmul_grad", shape, dtype))
+    want, part = normal + z64 * density, np.abs(z64) * density
+    error = normal * phi + part * half * (1.5 * z64 ** 2 + 8) + half * (normal + part)
+    # rounded twice in bf16: as the operand of the product with 1, and as its result, which is the same value
+    U.check(grad.view(n), want, error + U.HALF[dtype] * (np.abs(want) + error), "slope")
+
+
 def test_rows_far_behind_32_bits(cs):
     """Rows whose byte offsets in their buffers pass 2^32, through dispatch,
     product, gradients and combine."""
