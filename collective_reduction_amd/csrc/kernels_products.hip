@@ -1118,8 +1118,8 @@ __global__ __launch_bounds__(512) void bias_kernel(BiasArgs a) {
 // ---------------------------------------------------------------------------
 // A copy of a matrix's rows with a stride of whole 16-byte vectors, zeros
 // behind each row's end: rows that do not start on 16 bytes cannot be loaded
-// straight to LDS.  A wave per row; of a rank's rows only the first
-// offsets[r][per_rank], where the rows are the experts' tokens.
+// straight to LDS.  A wave per row; where the rows are the experts' tokens,
+// only those up to the largest of the rank's offsets.
 // ---------------------------------------------------------------------------
 struct PackArgs {
   RankPtrs in, offsets;
@@ -1133,7 +1133,21 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs a) {
   constexpr int V = 16 / int(sizeof(S)), U = 4;
   const uint32_t rank = blockIdx.y;
   uint32_t rows = a.rows;
-  if (a.ragged) rows = offset_at(static_cast<const int*>(a.offsets.get(int(rank))), a.per_rank, a.rows);
+  if (a.ragged) {
+    // the last offset, unless offsets decrease: an expert before may end later
+    const int* off = static_cast<const int*>(a.offsets.get(int(rank)));
+    rows = 0;
+    for (uint32_t e = uint32_t(lane_id()); e <= a.per_rank; e += kWave) {
+      const uint32_t v = offset_at(off, e, a.rows);
+      rows = v > rows ? v : rows;
+    }
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d /= 2) {
+      const uint32_t v = uint32_t(__shfl_xor(int(rows), d));
+      rows = v > rows ? v : rows;
+    }
+    rows = uniform(rows);
+  }
   const S* in = static_cast<const S*>(a.in.get(int(rank)));
   S* out = static_cast<S*>(a.out) + uint64_t(rank) * a.rows * a.ld;
   for (uint32_t r = blockIdx.x * 4 + uint32_t(wave_id()); r < rows; r += gridDim.x * 4) {

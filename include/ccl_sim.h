@@ -628,8 +628,9 @@ ccl_sim_result_t ccl_sim_expert_combine_grad(const ccl_sim_expert_shape_t* shape
  * dtype float32 or bf16, of every buffer but offsets; bf16 products are
  * summed in float32 and rounded once.  offsets NULL (experts == nranks
  * only): every one of the capacity rows belongs to the rank's one expert,
- * a plain dense product per rank.  Offsets outside [0, capacity] or
- * decreasing are read as empty or cut ranges, never past a buffer.
+ * a plain dense product per rank.  Offsets outside [0, capacity] are read as
+ * the nearer end of it, and a range whose end lies before its start as empty;
+ * of ranges that overlap the results are unspecified, within the buffers.
  * out[r] may be residual[r] itself.  hidden must be at least 1.
  */
 ccl_sim_result_t ccl_sim_expert_matmul(const ccl_sim_expert_shape_t* shape, const void* const* rows,

@@ -503,6 +503,33 @@ def test_bad_offsets_stay_inside_the_buffers(cs):
     assert bool((grad_w[:, 1] == 0).all()) and bool((grad_w[:, 3] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_offsets_that_decrease_leave_the_earlier_ranges_whole(cs, dtype):
+    """An expert whose range ends before it starts is empty; the one before it
+    keeps all its rows, also where they are copied with aligned rows first."""
+    capacity, hidden, features, t = 4100, 1031, 1025, U.TORCH[dtype]
+    rng, _, x64, x, w64, w = product_inputs(1, 2, capacity, hidden, features, dtype)
+    g64, g = U.values(rng, (1, capacity, features), dtype)
+    off, good = np.array([[0, 4000, 100]], np.int32), np.array([[0, 4000, 4000]], np.int32)
+    shape = cs.ExpertShape(nranks=1, experts=2, capacity=capacity, hidden=hidden, features=features)
+
+    def workspace(op):
+        ws = cs.ExpertWorkspace(op, shape, dtype)
+        ws.tensor.fill_(255)
+        return ws
+
+    out = torch.zeros(1, capacity, features, dtype=t, device="cuda")
+    cs.ccl_sim_expert_matmul(shape, dev(x), dev(w), out, offsets=dev(off), workspace=workspace("matmul"))
+    want, _, size = X.matmul(x64, good, w64)
+    U.check(out, want, U.sum_bound(size, hidden, dtype, want), "out")
+    grad_rows, grad_w = torch.zeros(1, capacity, hidden, dtype=t, device="cuda"), torch.empty_like(w, device="cuda")
+    cs.ccl_sim_expert_matmul_grad(shape, dev(g), rows=dev(x), weights=dev(w), offsets=dev(off), grad_rows=grad_rows,
+                                  grad_weights=grad_w, workspace=workspace("matmul_grad"))
+    got = X.matmul_grad(g64, x64, good, w64)
+    U.check(grad_rows, got["rows"][0], U.sum_bound(got["rows"][1], features, dtype, got["rows"][0]), "grad_rows")
+    U.check(grad_w, got["weights"][0], U.sum_bound(got["weights"][1], capacity, dtype, got["weights"][0]), "grad_weights")
+
+
 # --------------------------------------------------------------------------
 # together
 # --------------------------------------------------------------------------
