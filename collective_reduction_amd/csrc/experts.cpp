@@ -232,6 +232,7 @@ ProductCall product_call(const Shape& s, int dtype, int activation, ccl_sim_stre
   c.capacity = uint32_t(s.capacity);
   c.hidden = uint32_t(s.hidden);
   c.features = uint32_t(s.features);
+  c.log_plan = debug_enabled();
   c.stream = reinterpret_cast<hipStream_t>(stream);
   return c;
 }

@@ -52,6 +52,7 @@ struct ProductCall {
   RankPtrs grads{}, grad_rows{}, grad_weights{}, grad_bias{};
   bool rows16 = false, weights16 = false, grads16 = false;  // every rank's buffer starts on 16 bytes
   char* scratch = nullptr;     // the plan's parts of the workspace
+  bool log_plan = false;       // each product's form to stderr
   hipStream_t stream = nullptr;
   int num_cus = 0;
 };

@@ -44,6 +44,8 @@
 // row: the bias, the residual and the stores move whole 16-byte vectors,
 // four lanes a 128-byte line.
 
+#include <cstdio>
+
 #include "experts.hpp"
 #include "kernel_common.hpp"
 
@@ -1229,7 +1231,7 @@ struct Operand {
 constexpr uint64_t kMostBlocks = uint64_t(1) << 22;
 
 template <class T, int MODE>
-hipError_t launch_product(ProductArgs a, const Operand& x, const Operand& y, hipStream_t stream, int num_cus) {
+hipError_t launch_product(const ProductCall& c, ProductArgs a, const Operand& x, const Operand& y) {
   using S = typename T::S;
   const uint32_t size = sizeof(S);
   a.a = *x.ranks;
@@ -1254,12 +1256,17 @@ hipError_t launch_product(ProductArgs a, const Operand& x, const Operand& y, hip
       // as many workgroups as run at once, or as there may be tiles
       const uint64_t mtiles = a.has_offsets ? a.capacity / bm + a.per_rank : (a.capacity + bm - 1) / bm;
       const uint64_t most = (uint64_t(a.nranks) * mtiles * a.ntiles + 7) / 8 * 8;
-      grid = uint64_t(num_cus) * per_cu / 8 * 8;
+      grid = uint64_t(c.num_cus) * per_cu / 8 * 8;
       if (grid < 8) grid = 8;
       if (most < grid) grid = most;
     }
     if (grid == 0) return hipSuccess;
-    hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(threads), 0, stream, a);
+    if (c.log_plan)
+      std::fprintf(stderr, "[ccl_sim] product %s %s: tiles of %u x %u by %u threads, loads %s, %llu workgroups\n",
+                   MODE == kForward ? "forward" : MODE == kGradRows ? "grad_rows" : "grad_weights",
+                   size == 2 ? "bf16" : "float32", bm, bn, threads, direct ? "to LDS" : "by registers",
+                   static_cast<unsigned long long>(grid));
+    hipLaunchKernelGGL(kernel, dim3(unsigned(grid)), dim3(threads), 0, c.stream, a);
     return hipGetLastError();
   };
   // The tile: the largest that gives every compute unit at least one.  What
@@ -1272,7 +1279,7 @@ hipError_t launch_product(ProductArgs a, const Operand& x, const Operand& y, hip
     if (MODE == kGradWeights) return experts * a.splits * ((a.m + bm - 1) / bm) * wide;
     return experts * ((a.capacity / a.per_rank + bm - 1) / bm) * wide;
   };
-  const uint64_t cus = uint64_t(num_cus);
+  const uint64_t cus = uint64_t(c.num_cus);
   if (!direct) {
     // Rows off the 16-byte grid, loaded through registers: what counts is
     // having other waves to run while a stage's loads arrive, so 8 waves
@@ -1369,6 +1376,8 @@ hipError_t matmul(const ProductCall& c) {
     few.b = c.weights;
     few.ntiles = (a.n + kWaveN - 1) / kWaveN;
     const dim3 grid(a.nranks * a.per_rank * few.ntiles);
+    if (c.log_plan)
+      std::fprintf(stderr, "[ccl_sim] product forward %s: few rows, %u workgroups\n", sizeof(S) == 2 ? "bf16" : "float32", grid.x);
     hipLaunchKernelGGL(few_rows_kernel<T>, grid, dim3(256), 0, c.stream, few);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.least == 0) return e;
@@ -1380,7 +1389,7 @@ hipError_t matmul(const ProductCall& c) {
     if (e == hipSuccess) e = pack<S>(c, w, plan.weights, c.per_rank * c.features, c.hidden, plan.ldh, false);
     if (e != hipSuccess) return e;
   }
-  return launch_product<T, kForward>(a, x, w, c.stream, c.num_cus);
+  return launch_product<T, kForward>(c, a, x, w);
 }
 
 template <class T>
@@ -1444,7 +1453,7 @@ hipError_t matmul_grad(const ProductCall& c) {
     a.out = c.grad_rows;
     a.n = c.hidden;
     a.k = c.features;
-    e = launch_product<T, kGradRows>(a, dz, w, c.stream, c.num_cus);
+    e = launch_product<T, kGradRows>(c, a, dz, w);
     if (e != hipSuccess) return e;
   }
   if (c.want_weights && c.features > 0) {
@@ -1459,7 +1468,7 @@ hipError_t matmul_grad(const ProductCall& c) {
     a.n = c.hidden;
     a.splits = plan.splits;
     a.parts = reinterpret_cast<float*>(c.scratch + plan.parts);
-    e = launch_product<T, kGradWeights>(a, dz, x, c.stream, c.num_cus);
+    e = launch_product<T, kGradWeights>(c, a, dz, x);
     if (e != hipSuccess || plan.splits == 1) return e;
     JoinArgs j{};
     j.out = c.grad_weights;

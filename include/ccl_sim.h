@@ -80,11 +80,13 @@
  *            and the per-device scratch of ccl_sim_allreduce_noalloc; calls
  *            with distinct workspaces may run concurrently.
  * Debug.     With the environment variable CCL_SIM_DEBUG=1 (read on every
- *            call) each call logs its launch plan to stderr, and before a
- *            ring or recursive call that keeps partials in the workspace
- *            the library fills their part of it with all-ones bits (a NaN
- *            as float32, -1 as an integer) on the call's stream, so that a
- *            partial read before it is written shows in the result.
+ *            call) each call logs its launch plan to stderr (the experts'
+ *            products the kernel form of each launch too), and before a
+ *            ring or recursive call, or an expert call, that keeps partials
+ *            or copies in the workspace the library fills their part of it
+ *            with all-ones bits (a NaN as float32, -1 as an integer) on the
+ *            call's stream, so that a read of what the call has not written
+ *            shows in the result.
  */
 #ifndef CCL_SIM_H
 #define CCL_SIM_H

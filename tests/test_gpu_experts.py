@@ -310,6 +310,84 @@ def test_product_gradients_match_the_oracle(cs, n, per_rank, capacity, hidden, f
         U.check(got[name], value, bound, name)
 
 
+# The forms of the tile kernel, each with a shape that the dispatch gives it on 256 compute units: two experts of about
+# capacity / 2 rows.  What decides is the number of tiles, of 256 x 256 (bf16, from
+# 256 on), 128 x 128 (bf16 from 320, float32 from 256) and 64 x 128 (bf16, and whatever loads by registers, from 192).
+FORMS = [  # mode, dtype, capacity, hidden, features, elements off the 16-byte grid, the form
+    ("forward", "bfloat16", 4100, 72, 4104, 0, "256 x 256 by 512 threads, loads to LDS"),
+    ("forward", "bfloat16", 2600, 72, 2056, 0, "128 x 128 by 256 threads, loads to LDS"),
+    ("forward", "bfloat16", 1300, 200, 1288, 0, "64 x 128 by 256 threads, loads to LDS"),
+    ("forward", "bfloat16", 300, 136, 264, 0, "64 x 64 by 256 threads, loads to LDS"),
+    ("forward", "bfloat16", 2600, 73, 2057, 0, "64 x 128 by 512 threads, loads by registers"),
+    ("forward", "bfloat16", 2600, 72, 2056, 1, "64 x 128 by 512 threads, loads by registers"),
+    ("forward", "bfloat16", 300, 131, 265, 0, "64 x 64 by 256 threads, loads by registers"),
+    ("forward", "float32", 2300, 72, 2056, 0, "128 x 128 by 256 threads, loads to LDS"),
+    ("forward", "float32", 300, 136, 264, 0, "64 x 64 by 256 threads, loads to LDS"),
+    ("forward", "float32", 2600, 73, 2057, 0, "64 x 128 by 512 threads, loads by registers"),
+    ("forward", "float32", 300, 131, 265, 0, "64 x 64 by 256 threads, loads by registers"),
+    ("grad_rows", "bfloat16", 4100, 4104, 72, 0, "256 x 256 by 512 threads, loads to LDS"),
+    ("grad_rows", "bfloat16", 2600, 2056, 72, 0, "128 x 128 by 256 threads, loads to LDS"),
+    ("grad_rows", "bfloat16", 1300, 1288, 200, 0, "64 x 128 by 256 threads, loads to LDS"),
+    ("grad_rows", "bfloat16", 300, 264, 136, 0, "64 x 64 by 256 threads, loads to LDS"),
+    ("grad_rows", "bfloat16", 2600, 2057, 73, 0, "64 x 128 by 512 threads, loads by registers"),
+    ("grad_rows", "bfloat16", 2600, 2056, 72, 1, "64 x 128 by 512 threads, loads by registers"),
+    ("grad_rows", "bfloat16", 300, 265, 131, 0, "64 x 64 by 256 threads, loads by registers"),
+    ("grad_rows", "float32", 2300, 2056, 72, 0, "128 x 128 by 256 threads, loads to LDS"),
+    ("grad_rows", "float32", 300, 264, 136, 0, "64 x 64 by 256 threads, loads to LDS"),
+    ("grad_rows", "float32", 2600, 2057, 73, 0, "64 x 128 by 512 threads, loads by registers"),
+    ("grad_rows", "float32", 300, 265, 131, 0, "64 x 64 by 256 threads, loads by registers"),
+    ("grad_weights", "bfloat16", 180, 3000, 3016, 0, "256 x 256 by 512 threads, loads to LDS"),
+    ("grad_weights", "bfloat16", 180, 1800, 1560, 0, "128 x 128 by 256 threads, loads to LDS"),
+    ("grad_weights", "bfloat16", 180, 1000, 776, 0, "64 x 128 by 256 threads, loads to LDS"),
+    ("grad_weights", "bfloat16", 180, 200, 264, 0, "64 x 64 by 256 threads, loads to LDS"),
+    ("grad_weights", "bfloat16", 180, 1001, 777, 0, "64 x 128 by 512 threads, loads by registers"),
+    ("grad_weights", "bfloat16", 180, 1000, 776, 1, "64 x 128 by 512 threads, loads by registers"),
+    ("grad_weights", "bfloat16", 180, 201, 265, 0, "64 x 64 by 256 threads, loads by registers"),
+    ("grad_weights", "float32", 180, 1800, 1560, 0, "128 x 128 by 256 threads, loads to LDS"),
+    ("grad_weights", "float32", 180, 200, 264, 0, "64 x 64 by 256 threads, loads to LDS"),
+    ("grad_weights", "float32", 180, 1001, 777, 0, "64 x 128 by 512 threads, loads by registers"),
+    ("grad_weights", "float32", 180, 201, 265, 0, "64 x 64 by 256 threads, loads by registers"),
+]
+
+
+@pytest.mark.parametrize("mode,dtype,capacity,hidden,features,offset,form", FORMS)
+def test_every_form_of_the_tiles_is_reached_and_right(cs, capfd, monkeypatch, mode, dtype, capacity, hidden, features, offset, form):
+    """Debug mode says which form a launch takes (and fills the workspace with
+    NaN bits); a threshold that moves past one of these shapes shows here."""
+    if torch.cuda.get_device_properties(0).multi_processor_count != 256:
+        pytest.skip("the forms are chosen for 256 compute units")
+    monkeypatch.setenv("CCL_SIM_DEBUG", "1")
+    rng = np.random.default_rng([29, capacity, hidden, features])
+    ends = [capacity // 2 + 21, capacity - 17]
+    off = np.array([[0, *ends]], np.int32)
+    nobody = torch.from_numpy(~owned(off, capacity)[..., 0])
+    x64, x = U.values(rng, (1, capacity, hidden), dtype)
+    w64, w = U.values(rng, (1, 2, features, hidden), dtype, hidden ** -0.5)
+    g64, g = U.values(rng, (1, capacity, features), dtype)
+    for t in (x, g):
+        t[nobody] = float("nan")
+    x, w, g = (U.shifted(t, offset) for t in (x, w, g))
+    shape = cs.ExpertShape(nranks=1, experts=2, capacity=capacity, hidden=hidden, features=features)
+    ws = cs.ExpertWorkspace("matmul" if mode == "forward" else "matmul_grad", shape, dtype)
+    capfd.readouterr()
+    mine = owned(off, capacity)
+    if mode == "forward":
+        got = torch.full((1, capacity, features), 7.0, dtype=U.TORCH[dtype], device="cuda")
+        cs.ccl_sim_expert_matmul(shape, x, w, got, offsets=dev(off), activation="relu", workspace=ws)
+        want, _, size = X.matmul(x64, off, w64, None, None, "relu")
+        bound = U.sum_bound(size, hidden, dtype, want)
+    else:
+        got = torch.full((1, capacity, hidden) if mode == "grad_rows" else w.shape, 7.0, dtype=U.TORCH[dtype], device="cuda")
+        cs.ccl_sim_expert_matmul_grad(shape, g, offsets=dev(off), rows=x, weights=w, workspace=ws, **{mode: got})
+        want, size = X.matmul_grad(g64, x64, off, w64)[mode[5:]]
+        bound = U.sum_bound(size, features if mode == "grad_rows" else max(ends[0], ends[1] - ends[0]), dtype, want)
+    lines = [ln for ln in capfd.readouterr().err.splitlines() if ln.startswith("[ccl_sim] product")]
+    assert len(lines) == 1 and f"product {mode} " in lines[0] and f"tiles of {form}," in lines[0], lines
+    if mode != "grad_weights":
+        want, bound = np.where(mine, want, 7.0), np.where(mine, bound, 0)
+    U.check(got, want, bound, mode)
+
+
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("rows", [(0, 32, 1, 33, 0), (120, 0, 0, 0, 3), (17, 16, 15, 31, 40), (0, 0, 0, 0, 0)])
 def test_few_rows_on_average_and_many_of_one_expert(cs, dtype, rows):
