@@ -80,7 +80,7 @@ struct ProductArgs {
   uint32_t m, n, k;      // features and hidden as the mode uses them; m / k of the ragged axis unused
   uint32_t lda, ldb;     // row strides of the operands, in elements
   uint32_t splits;       // parts of k (weights' gradient)
-  uint32_t least;        // forward: experts with fewer rows are the other kernel's (0: none are)
+  uint32_t least;        // forward: experts with fewer rows are the form's for few rows (0: none are)
   uint32_t ntiles;       // tiles of n
   bool has_offsets, has_bias, has_residual, has_preact;
   int activation;
@@ -873,26 +873,29 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void product_kernel(ProductArgs a
 // expert; its four waves take turns along k, 128 bytes each, so a wave's 8
 // weight loads of a turn cover 64 whole lines, and the next turn's are
 // started before the products of this one.  The waves' sums are added in
-// LDS, in order, and wave j finishes the columns of fragment j.  16 rows are
-// multiplied per pass over the weights.  32 rows over 32 experts, 2048 ->
-// 4096 bf16 (405 MB): 71 us, 5.7 TB/s.
+// LDS, in order, and wave j finishes the columns of fragment j.  An expert has
+// at most the 16 rows of one fragment; those with more are left to the tiles.
+// 8 experts of 8 rows, 2048 -> 2048:
+// bf16 18 us (67 MB, 3.7 TB/s), float32 32 us (4.2 TB/s); 64 experts 2048 ->
+// 4096 float32 (2.1 GB) 523 us, 4.1 TB/s.
 // ---------------------------------------------------------------------------
+constexpr uint32_t kFewRows = 16;
+
 template <class T>
 __global__ __launch_bounds__(256) void few_rows_kernel(ProductArgs a) {
-  constexpr int MT = 1;  // groups of 16 rows per pass
   using S = typename T::S;
   using El = Elem<S>;
   using Chunk = typename VecOf<S, El::kChunk>::type;
-  __shared__ float4_t part[4][MT][4][kWave];
+  __shared__ float4_t part[4][4][kWave];
   const uint32_t block = blockIdx.x % a.ntiles, q = blockIdx.x / a.ntiles;
   const uint32_t rank = q / a.per_rank, expert = q - rank * a.per_rank;
   const int* off = a.has_offsets ? static_cast<const int*>(a.offsets.get(int(rank))) : nullptr;
   const Range r = rows_of(off, expert, a.capacity);
   const uint32_t lo = uniform(r.lo), rows = uniform(r.hi) - lo;
-  if (a.least > 0 && rows >= a.least) return;
+  if (rows == 0 || rows > kFewRows) return;
   const uint32_t l = uint32_t(lane_id()), i = l % 16, g = l / 16, w = uint32_t(wave_id());
   const uint32_t n0 = block * kWaveN;
-  // this lane's weight rows (one per fragment; past the last: the last, not stored) and its k within a half
+  // this lane's weight rows (one per fragment) and its row, and their k within a half; past the last the last, not stored
   const S* wrow[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -900,85 +903,64 @@ __global__ __launch_bounds__(256) void few_rows_kernel(ProductArgs a) {
     n = n < a.n ? n : a.n - 1;
     wrow[j] = static_cast<const S*>(a.b.get(int(rank))) + (uint64_t(expert) * a.n + n) * a.k + g * El::kChunk;
   }
-  for (uint32_t m0 = 0; m0 < rows; m0 += 16 * MT) {
-    const S* xrow[MT];
+  const S* xrow = static_cast<const S*>(a.a.get(int(rank))) + uint64_t(lo + (i < rows ? i : rows - 1)) * a.k + g * El::kChunk;
+  float4_t acc[4];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      uint32_t m = m0 + 16 * uint32_t(t) + i;
-      m = m < rows ? m : rows - 1;
-      xrow[t] = static_cast<const S*>(a.a.get(int(rank))) + uint64_t(lo + m) * a.k + g * El::kChunk;
+  for (int j = 0; j < 4; ++j) acc[j] = float4_t{0, 0, 0, 0};
+  struct Turn {
+    Chunk w[4][2], x[2];
+  };
+  // The loads of k from k0 on; `whole`: all of it inside k.
+  auto load = [&](Turn& u, uint32_t k0, bool whole) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t at = k0 + uint32_t(h) * (El::kStage / 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        u.w[j][h] = whole ? vload<S, El::kChunk, true>(wrow[j] + at) : cut(wrow[j] + at, at + g * El::kChunk, a.k);
+      u.x[h] = whole ? vload<S, El::kChunk, false>(xrow + at) : cut(xrow + at, at + g * El::kChunk, a.k);
     }
-    float4_t acc[MT][4];
+  };
+  auto products = [&](const Turn& u) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[t][j] = float4_t{0, 0, 0, 0};
-    struct Turn {
-      Chunk w[4][2], x[MT][2];
-    };
-    // The loads of k from k0 on; `whole`: all of it inside k.
-    auto load = [&](Turn& u, uint32_t k0, bool whole) {
+      for (int j = 0; j < 4; ++j)
+        acc[j] = multiply<T>(__builtin_bit_cast(float4_t, u.w[j][h]), __builtin_bit_cast(float4_t, u.x[h]), acc[j]);
+  };
+  constexpr uint32_t kTurn = 4 * El::kStage;
+  uint32_t k0 = w * El::kStage;
+  Turn now, next;
+  if (k0 + El::kStage <= a.k) load(now, k0, true);
+  for (; k0 + kTurn + El::kStage <= a.k; k0 += kTurn) {
+    load(next, k0 + kTurn, true);
+    products(now);
+    now = next;
+  }
+  if (k0 + El::kStage <= a.k) {
+    products(now);
+    k0 += kTurn;
+  }
+  if (k0 < a.k) {
+    load(now, k0, false);
+    products(now);
+  }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t at = k0 + uint32_t(h) * (El::kStage / 2);
+  for (int j = 0; j < 4; ++j) part[w][j][l] = acc[j];
+  __syncthreads();
+  const uint32_t n = n0 + g * 16 + w * 4;
+  const float4_t sum = (part[0][w][l] + part[1][w][l]) + (part[2][w][l] + part[3][w][l]);
+  if (i >= rows) return;
+  const uint64_t at = uint64_t(lo + i) * a.n + n;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          u.w[j][h] = whole ? vload<S, El::kChunk, true>(wrow[j] + at) : cut(wrow[j] + at, at + g * El::kChunk, a.k);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          u.x[t][h] = whole ? vload<S, El::kChunk, false>(xrow[t] + at) : cut(xrow[t] + at, at + g * El::kChunk, a.k);
-      }
-    };
-    auto products = [&](const Turn& u) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[t][j] = multiply<T>(__builtin_bit_cast(float4_t, u.w[j][h]), __builtin_bit_cast(float4_t, u.x[t][h]), acc[t][j]);
-    };
-    constexpr uint32_t kTurn = 4 * El::kStage;
-    uint32_t k0 = w * El::kStage;
-    Turn now, next;
-    if (k0 + El::kStage <= a.k) load(now, k0, true);
-    for (; k0 + kTurn + El::kStage <= a.k; k0 += kTurn) {
-      load(next, k0 + kTurn, true);
-      products(now);
-      now = next;
-    }
-    if (k0 + El::kStage <= a.k) {
-      products(now);
-      k0 += kTurn;
-    }
-    if (k0 < a.k) {
-      load(now, k0, false);
-      products(now);
-    }
-    __syncthreads();  // the previous rows' sums have been read
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) part[w][t][j][l] = acc[t][j];
-    __syncthreads();
-    const uint32_t n = n0 + g * 16 + w * 4;
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const float4_t sum = (part[0][t][w][l] + part[1][t][w][l]) + (part[2][t][w][l] + part[3][t][w][l]);
-      const uint32_t m = m0 + 16 * uint32_t(t) + i;
-      if (m >= rows) continue;
-      const uint64_t at = uint64_t(lo + m) * a.n + n;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (n + u >= a.n) continue;
-        float v = sum[u];
-        if (a.has_bias) v += T::widen(get1(static_cast<const S*>(a.bias.get(int(rank))) + uint64_t(expert) * a.n + n + u));
-        if (a.has_preact) put1(static_cast<S*>(const_cast<void*>(a.preact.get(int(rank)))) + at + u, round_to<T>(v));
-        v = activate<T>(v, a.activation);
-        if (a.has_residual) v += T::widen(get1(static_cast<const S*>(a.residual.get(int(rank))) + at + u));
-        put1(static_cast<S*>(const_cast<void*>(a.out.get(int(rank)))) + at + u, round_to<T>(v));
-      }
-    }
+  for (int u = 0; u < 4; ++u) {
+    if (n + u >= a.n) continue;
+    float v = sum[u];
+    if (a.has_bias) v += T::widen(get1(static_cast<const S*>(a.bias.get(int(rank))) + uint64_t(expert) * a.n + n + u));
+    if (a.has_preact) put1(static_cast<S*>(const_cast<void*>(a.preact.get(int(rank)))) + at + u, round_to<T>(v));
+    v = activate<T>(v, a.activation);
+    if (a.has_residual) v += T::widen(get1(static_cast<const S*>(a.residual.get(int(rank))) + at + u));
+    put1(static_cast<S*>(const_cast<void*>(a.out.get(int(rank)))) + at + u, round_to<T>(v));
   }
 }
 
@@ -1345,13 +1327,6 @@ ProductPlan plan_of(const ProductCall& c) {
   return product_plan(c.dtype, uint32_t(c.nranks), c.per_rank, c.capacity, c.hidden, c.features);
 }
 
-// At most this many rows per expert on average: the weights are read once,
-// straight into the fragments.  Measured in bf16, 2048 -> 4096, that form /
-// the tiles of 64 rows: one row each of 32 experts, whose weights come from
-// memory, 75 / 80 us; of 8 experts, whose weights stay in the Infinity Cache,
-// 1 row 34 / 26, 16 rows 37 / 27, 64 rows 58 / 29.
-constexpr uint32_t kFewRows = 8, kMostFewRows = 32;
-
 template <class T>
 hipError_t matmul(const ProductCall& c) {
   using S = typename T::S;
@@ -1367,14 +1342,33 @@ hipError_t matmul(const ProductCall& c) {
   a.has_preact = c.has_preact;
   a.activation = c.activation;
   const uint32_t rows = c.capacity / c.per_rank;
-  if (rows <= kFewRows) {
-    // an expert may still have many: those above kMostFewRows are left to the
-    // tiles, where the capacity allows for any
-    if (c.capacity > kMostFewRows && c.has_offsets) a.least = kMostFewRows + 1;
+  // The form for few rows: up to one pass of 16 rows over the weights per expert
+  // on average, where its workgroups (64 columns of an expert each) are no more
+  // than the compute units, and of float32 with rows on the 16-byte grid also
+  // where there are more.  Measured (us, tiles / few rows; weights from memory
+  // and, in brackets, from the caches):
+  //   workgroups, bf16, 8 rows an expert: 64 (2048 -> 4096) 30 / 15 [17 / 13],
+  //     128 19 / 10 [13 / 10], 256 (2048 -> 2048) 32 / 18 [23 / 17], 256 (5120 ->
+  //     4096) 66 / 43 [45 / 42]; 320 34 / 29 [23 / 28], 512 40 / 35 [27 / 33],
+  //     1,024 30 / 33 [26 / 32], 2,560 138 / 158, 5120 -> 2560 with 1,280 160 / 205;
+  //     of odd widths 65 (4097 -> 4097) 68 / 64 [52 / 64], 256 40 / 30 [31 / 29],
+  //     512 49 / 54; in between it is by the shape: 2048 -> 4096 with 2,048 127 /
+  //     120, 32 rows over those 32 experts at random 77 / 70
+  //   float32: 256 58 / 32 [49 / 31], 512 82 / 66, 1,024 87 / 70, 4,096 289 / 254;
+  //     of odd widths 256 66 / 42, 512 91 / 88, 1,024 85 / 93
+  //   rows an expert, 256 workgroups, bf16: 16 32 / 19 [23 / 18], 32 32 / 34 [23 / 33];
+  //     float32: 16 58 / 33 [49 / 33], 32 58 / 64 [49 / 64]
+  const uint32_t columns = (a.n + kWaveN - 1) / kWaveN;
+  const bool narrow = uint64_t(a.nranks) * a.per_rank * columns <= uint64_t(c.num_cus);
+  const bool wide = sizeof(S) == 4 && c.rows16 && c.weights16 && c.hidden * sizeof(S) % 16 == 0;
+  if (rows <= kFewRows && (narrow || wide)) {
+    // An expert may still have more: those are left to the tiles, in a second
+    // launch where the capacity allows for any (2.5 us when there are none).
+    if (c.capacity > kFewRows && c.has_offsets) a.least = kFewRows + 1;
     ProductArgs few = a;
     few.a = c.rows;
     few.b = c.weights;
-    few.ntiles = (a.n + kWaveN - 1) / kWaveN;
+    few.ntiles = columns;
     const dim3 grid(a.nranks * a.per_rank * few.ntiles);
     if (c.log_plan)
       std::fprintf(stderr, "[ccl_sim] product forward %s: few rows, %u workgroups\n", sizeof(S) == 2 ? "bf16" : "float32", grid.x);

@@ -408,6 +408,47 @@ def test_few_rows_on_average_and_many_of_one_expert(cs, dtype, rows):
     U.check(out, np.where(mine, want, 7.0), np.where(mine, U.product_bound(z, size, hidden, dtype, "silu", None, want), 0), "out")
 
 
+@pytest.mark.parametrize("dtype,n,per_rank,capacity,hidden,features,rows,forms", [
+    # as many workgroups as compute units, and more; rows that may be over the form's 16, and are
+    ("bfloat16", 2, 2, 32, 200, 4096, (16, 16), ("few", "tiles")), ("bfloat16", 2, 2, 32, 200, 4097, (15, 17), ("tiles",)),
+    ("bfloat16", 2, 2, 33, 131, 4095, (1, 32), ("few", "tiles")), ("float32", 2, 2, 32, 72, 4097, (17, 15), ("few", "tiles")),
+    ("float32", 2, 2, 32, 73, 4097, (9, 16), ("tiles",)), ("float32", 2, 2, 32, 73, 4095, (9, 16), ("few", "tiles")),
+    # no room for more than 16, with offsets and without; one row over
+    ("bfloat16", 3, 1, 16, 136, 72, (16,), ("few",)), ("float32", 3, 1, 16, 136, 72, None, ("few",)),
+    ("bfloat16", 3, 1, 16, 4104, 72, None, ("few",)), ("bfloat16", 3, 1, 17, 136, 72, None, ("tiles",)),
+    ("float32", 3, 2, 34, 136, 72, (16, 18), ("tiles",)),
+    # many experts of few rows and one of many
+    ("bfloat16", 1, 50, 800, 264, 130, (0, 700, 1, 16, 17, 0, 33), ("few", "tiles")),
+    ("float32", 1, 50, 800, 264, 130, (16, 1, 17, 0, 650), ("few", "tiles")),
+])
+def test_the_form_for_few_rows_and_its_limits(cs, capfd, monkeypatch, dtype, n, per_rank, capacity, hidden, features, rows, forms):
+    if torch.cuda.get_device_properties(0).multi_processor_count != 256:
+        pytest.skip("the forms are chosen for 256 compute units")
+    monkeypatch.setenv("CCL_SIM_DEBUG", "1")
+    rng = np.random.default_rng([31, capacity, hidden, features])
+    off = np.tile(np.array([[0, capacity]], np.int32), (n, 1))
+    if rows is not None:
+        counts = np.zeros((n, per_rank), np.int64)
+        counts[:, :len(rows)] = rows
+        off = np.concatenate([np.zeros((n, 1), np.int64), np.cumsum(counts, 1)], 1).astype(np.int32)
+    x64, x = U.values(rng, (n, capacity, hidden), dtype)
+    w64, w = U.values(rng, (n, per_rank, features, hidden), dtype, hidden ** -0.5)
+    b64, b = U.values(rng, (n, per_rank, features), dtype)
+    res64, res = U.values(rng, (n, capacity, features), dtype)
+    mine = owned(off, capacity)
+    x[torch.from_numpy(~mine[..., 0])] = float("nan")
+    out, z = (torch.full((n, capacity, features), 7.0, dtype=U.TORCH[dtype], device="cuda") for _ in range(2))
+    shape = cs.ExpertShape(nranks=n, experts=n * per_rank, capacity=capacity, hidden=hidden, features=features)
+    capfd.readouterr()
+    cs.ccl_sim_expert_matmul(shape, dev(x), dev(w), out, offsets=None if rows is None else dev(off), bias=dev(b), residual=dev(res),
+                             preact=z, activation="gelu", workspace=cs.ExpertWorkspace("matmul", shape, dtype))
+    lines = [ln for ln in capfd.readouterr().err.splitlines() if ln.startswith("[ccl_sim] product forward")]
+    assert tuple("few" if "few rows" in ln else "tiles" for ln in lines) == forms, lines
+    want, want_z, size = X.matmul(x64, off, w64, b64, res64, "gelu")
+    U.check(out, np.where(mine, want, 7.0), np.where(mine, U.product_bound(want_z, size, hidden, dtype, "gelu", res64, want), 0), "out")
+    U.check(z, np.where(mine, want_z, 7.0), np.where(mine, U.sum_bound(size, hidden, dtype, want_z), 0), "preact")
+
+
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_a_row_that_is_no_number_stays_alone(cs, dtype):
     rng, off, x64, x, w64, w = product_inputs(1, 1, 300, 192, 264, dtype, dense=True)
