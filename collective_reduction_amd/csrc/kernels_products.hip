@@ -258,8 +258,9 @@ __device__ inline uint32_t uniform(uint32_t v) { return uint32_t(__builtin_amdgc
 // One 16-byte load per lane from a buffer straight into LDS: lane l's lands
 // at lds + 16·l.  In assembly, since the compiler orders every later LDS read
 // behind such a load it knows of; here the waits are the kernel's own.  The
-// instruction has no register result; m0 holds the LDS address, and nothing
-// else in these kernels uses m0.
+// instruction has no register result; m0 holds the LDS address.  m0 is
+// reserved: the compiler keeps no value of its own in it (and refuses it as a
+// clobber), and a test of the assembly holds that nothing else here uses it.
 __device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t rs, uint32_t lds, uint32_t offset, uint32_t more) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"

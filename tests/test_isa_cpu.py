@@ -60,3 +60,18 @@ def test_kernel_assembly_properties(assembly, name):
         assert not sizes
         return
     assert sizes and max(sizes) == 0, f"private segment sizes {sorted(set(sizes))}"
+
+
+def test_the_loads_to_lds_have_m0_to_themselves(assembly):
+    """The products' loads straight to LDS take their LDS address from m0,
+    set in the same assembly block; nothing else in that file reads or writes
+    m0, so no value of the compiler's is lost there."""
+    lines = [ln.split("//")[0].split(";")[0].strip() for ln in assembly["kernels_products.hip"].splitlines()]
+    lines = [ln for ln in lines if ln and not ln.startswith(".")]
+    users = [i for i, ln in enumerate(lines) if re.search(r"\bm0\b", ln)]
+    assert users
+    for i in users:
+        assert re.fullmatch(r"s_mov_b32 m0, (s\d+|vcc_lo|vcc_hi)", lines[i]), lines[i]
+        assert lines[i + 1] == "s_nop 0" and re.fullmatch(r"buffer_load_dwordx4 .* offen lds", lines[i + 2]), lines[i:i + 3]
+    loads = [ln for ln in lines if re.search(r"\blds\b", ln) and ln.startswith("buffer_load")]
+    assert len(loads) == len(users)
