@@ -21,6 +21,23 @@ def choices(rng, n, tokens, topk, experts, padded=0.1):
     return ids
 
 
+def route_sorted(ids, experts, capacity):
+    """X.route by one stable sort, for many choices."""
+    n, per_rank = ids.shape[0], experts // ids.shape[0]
+    flat = ids.reshape(-1).astype(np.int64)
+    key = np.where((flat >= 0) & (flat < experts), flat, experts)
+    order = np.argsort(key, kind="stable")
+    ends = np.cumsum(np.bincount(key, minlength=experts + 1)[:experts])
+    starts = np.concatenate([[0], ends])[::per_rank]  # rows of the ranks before; of all, for no choice
+    rank = key // per_rank
+    row = np.empty_like(key)
+    row[order] = np.arange(len(key))
+    row -= starts[np.minimum(rank, n)]
+    places = np.where((key < experts) & (row < capacity), rank * capacity + row, -1)
+    offsets = np.minimum(np.concatenate([np.zeros((n, 1), np.int64), ends.reshape(n, -1) - starts[:n, None]], 1), capacity)
+    return places.reshape(ids.shape).astype(np.int32), offsets.astype(np.int32)
+
+
 def values(rng, shape, dtype, scale=1.0):
     """Normal values as the stored type holds them: (float64 array, device tensor maker)."""
     v = torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(TORCH[dtype])
@@ -90,5 +107,5 @@ def grad_bound(size, terms, dtype, activation, want):
     return error + HALF[dtype] * (np.abs(want) + error)
 
 
-__all__ = ["X", "np", "torch", "TORCH", "HALF", "EPS", "choices", "values", "ranges", "shifted", "check", "sum_bound",
+__all__ = ["X", "np", "torch", "TORCH", "HALF", "EPS", "choices", "route_sorted", "values", "ranges", "shifted", "check", "sum_bound",
            "product_bound", "grad_bound"]

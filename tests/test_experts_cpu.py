@@ -256,6 +256,14 @@ def test_oracle_route_is_a_stable_sort(seed):
     assert (places[ids < 0] == -1).all()
 
 
+@pytest.mark.parametrize("n,experts,topk,tokens,capacity", [(3, 6, 2, 5, 7), (1, 9, 3, 40, 30), (4, 4, 1, 50, 60), (2, 8, 2, 0, 3)])
+def test_route_by_sort_is_the_oracles(n, experts, topk, tokens, capacity):
+    from expert_util import choices, route_sorted
+    ids = choices(np.random.default_rng([n, experts, tokens]), n, tokens, topk, experts)
+    for got, want in zip(route_sorted(ids, experts, capacity), X.route(ids, experts, capacity)):
+        assert got.dtype == want.dtype and np.array_equal(got, want)
+
+
 def test_oracle_exchange_round_trip_and_gradients_by_differences():
     rng, ids, n, per_rank, topk, tokens, capacity = small_case(9)
     places, _ = X.route(ids, n * per_rank, capacity)

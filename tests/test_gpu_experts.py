@@ -56,6 +56,25 @@ def test_route_matches_the_oracle(cs, n, experts, topk, tokens, capacity, id_dty
     assert np.array_equal(offsets.cpu().numpy(), want_offsets)
 
 
+LONG_ROUTES = [
+    # up to 4,096 choices in one launch (1,024 experts at most), from 4,097 on in three
+    (1, 64, 1, 4096, 4200), (4, 1024, 4, 256, 300), (1, 64, 1, 4097, 4200), (4, 1028, 4, 256, 300),
+    # 64 workgroups of 512 choices are one turn of the scan over them: one less, just that, one more; several turns
+    (1, 16, 1, 32767, 30000), (1, 16, 1, 32768, 30000), (1, 16, 1, 32769, 40000), (8, 64, 4, 4096, 18000), (3, 2046, 8, 4100, 40000),
+    # 2^20 - 1 choices by workgroups of 512, 2^20 and 2^20 + 1 of 4,096, and many of those
+    (3, 6, 5, 69905, 400000), (8, 64, 2, 65536, 140000), (17, 34, 1, 61681, 70000), (4, 100, 8, 65536, 600000),
+]
+
+
+@pytest.mark.parametrize("n,experts,topk,tokens,capacity", LONG_ROUTES)
+def test_route_of_many_choices(cs, n, experts, topk, tokens, capacity):
+    ids = U.choices(np.random.default_rng([37, n, experts, topk, tokens]), n, tokens, topk, experts)
+    _, places, offsets = run_route(cs, ids, experts, capacity)
+    want_places, want_offsets = U.route_sorted(ids, experts, capacity)
+    assert np.array_equal(places.cpu().numpy(), want_places)
+    assert np.array_equal(offsets.cpu().numpy(), want_offsets)
+
+
 def test_route_without_any_choice_and_with_one_expert_only(cs):
     for fill in (-1, 9, 2):
         ids = np.full((3, 50, 2), fill, np.int32)
