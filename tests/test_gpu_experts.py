@@ -408,6 +408,40 @@ def test_every_form_of_the_tiles_is_reached_and_right(cs, capfd, monkeypatch, mo
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("per_rank,capacity,hidden,features", [
+    (2, 65700, 40, 72), (1, 40000, 33, 65), (3, 20011, 264, 136)])
+def test_sums_over_many_rows_lose_none(cs, dtype, per_rank, capacity, hidden, features):
+    """Weights' and bias's gradients whose rows are split over workgroups (64, 78 and 13 times), of
+    whole numbers from -1 to 1 and sparse: every partial sum is a whole number
+    far below 2^24, so float32 sums are exact in any order, and a row too few
+    or twice is seen.  bf16 rounds the whole number once, to nearest even."""
+    rng = np.random.default_rng([41, capacity])
+    ends = np.sort(rng.integers(0, capacity + 1, per_rank - 1))
+    off = np.array([[0, *ends, capacity - 3]], np.int32)
+    x, g = (rng.integers(-1, 2, (1, capacity, n)) for n in (hidden, features))
+    t = U.TORCH[dtype]
+    grad_w = torch.full((1, per_rank, features, hidden), float("nan"), dtype=t, device="cuda")
+    grad_b = torch.full((1, per_rank, features), float("nan"), dtype=t, device="cuda")
+    shape = cs.ExpertShape(nranks=1, experts=per_rank, capacity=capacity, hidden=hidden, features=features)
+    ws = cs.ExpertWorkspace("matmul_grad", shape, dtype)
+    ws.tensor.fill_(255)
+    cs.ccl_sim_expert_matmul_grad(shape, dev(g.astype(np.float32), dtype), rows=dev(x.astype(np.float32), dtype), offsets=dev(off),
+                                  grad_weights=grad_w, grad_bias=grad_b, workspace=ws)
+    for e in range(per_rank):
+        lo, hi = off[0, e], off[0, e + 1]
+        want_w = (g[0, lo:hi].T.astype(np.float64) @ x[0, lo:hi].astype(np.float64))
+        want_b = g[0, lo:hi].sum(0)
+        assert np.abs(want_w).max(initial=0) < 1 << 23 and np.abs(want_b).max(initial=0) < 1 << 23
+        rounded = lambda v: torch.from_numpy(v.astype(np.float32)).to(t)  # noqa: E731
+        for got, want in ((grad_w[0, e], want_w), (grad_b[0, e], want_b)):
+            assert torch.equal(got.cpu(), rounded(want)), e
+        last = next(s for s in range(hi - 1, lo - 1, -1) if x[0, s].any() and g[0, s].any()) if hi > lo else None
+        if last is not None:  # the rounding hides no row
+            assert not torch.equal(rounded(want_w), rounded(want_w - np.outer(g[0, last], x[0, last])))
+            assert not torch.equal(rounded(want_b), rounded(want_b - g[0, last]))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("rows", [(0, 32, 1, 33, 0), (120, 0, 0, 0, 3), (17, 16, 15, 31, 40), (0, 0, 0, 0, 0)])
 def test_few_rows_on_average_and_many_of_one_expert(cs, dtype, rows):
     per_rank, hidden, features = 16, 200, 136
