@@ -855,3 +855,54 @@ def test_two_layers_at_once_on_two_streams(cs):
     for v, f in zip((one, two), first):
         for k in v.outputs:
             assert torch.equal(getattr(v, k), f[k]), k
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_shapes_in_debug_mode(cs, monkeypatch, seed):
+    """Products and their gradients of drawn shapes, odd and even, on and off
+    the vector grid, the workspace full of NaN bits, every row of no expert
+    too, against the oracle."""
+    monkeypatch.setenv("CCL_SIM_DEBUG", "1")
+    rng = np.random.default_rng([43, seed])
+    for _ in range(6):
+        size = lambda lo, hi: int(round(np.exp(rng.uniform(np.log(lo), np.log(hi)))))  # noqa: E731
+        n, per_rank, dtype = size(1, 6), size(1, 12), rng.choice(["float32", "bfloat16"])
+        capacity, hidden, features = size(1, 1500), size(1, 700), size(1, 700)
+        if rng.random() < 0.5:
+            hidden, features = -(-hidden // 8) * 8, -(-features // 8) * 8
+        act, offset = str(rng.choice(["none", "relu", "gelu", "silu"])), int(rng.random() < 0.25)
+        what = f"n={n} per_rank={per_rank} capacity={capacity} {hidden} -> {features} {dtype} {act} offset={offset}"
+        print(what, flush=True)
+        off = U.ranges(rng, n, per_rank, capacity)
+        mine = owned(off, capacity)
+        nobody = torch.from_numpy(~mine[..., 0])
+        x64, x = U.values(rng, (n, capacity, hidden), dtype)
+        w64, w = U.values(rng, (n, per_rank, features, hidden), dtype, hidden ** -0.5)
+        b64, b = U.values(rng, (n, per_rank, features), dtype)
+        res64, res = U.values(rng, (n, capacity, features), dtype)
+        g64, g = U.values(rng, (n, capacity, features), dtype)
+        z64, z = U.values(rng, (n, capacity, features), dtype)
+        for t in (x, g, z):
+            t[nobody] = float("nan")
+        x, w, g, z = (U.shifted(t, offset) for t in (x, w, g, z))
+        shape = cs.ExpertShape(nranks=n, experts=n * per_rank, capacity=capacity, hidden=hidden, features=features)
+        out = dev(res)
+        cs.ccl_sim_expert_matmul(shape, x, w, out, offsets=dev(off), bias=dev(b), residual=out, activation=act,
+                                 workspace=cs.ExpertWorkspace("matmul", shape, dtype))
+        want, want_z, total = X.matmul(x64, off, w64, b64, res64, act)
+        bound = U.product_bound(want_z, total, hidden, dtype, act, res64, want)
+        U.check(out, np.where(mine, want, res64), np.where(mine, bound, 0), what + " out")
+        got = {"rows": torch.full_like(x, 7.0), "weights": torch.full_like(w, float("nan")), "bias": torch.full_like(dev(b), float("nan"))}
+        cs.ccl_sim_expert_matmul_grad(shape, g, rows=x, weights=w, offsets=dev(off), preact=z if act != "none" else None,
+                                      activation=act, grad_rows=got["rows"], grad_weights=got["weights"], grad_bias=got["bias"],
+                                      workspace=cs.ExpertWorkspace("matmul_grad", shape, dtype))
+        want, flat = X.matmul_grad(g64, x64, off, w64, z64, act), X.matmul_grad(g64, x64, off, w64)
+        longest = int((off[:, 1:] - off[:, :-1]).max())
+        for name, terms in (("rows", features), ("weights", longest), ("bias", longest)):
+            value, total = want[name]
+            bound = U.grad_bound(total, terms, dtype, act if name != "bias" else "none", value)
+            if act != "none":  # as in test_product_gradients_match_the_oracle
+                bound = bound + 32 * U.EPS * flat[name][1] * (1 + np.abs(z64).max(initial=0))
+            if name == "rows":
+                value, bound = np.where(mine, value, 7.0), np.where(mine, bound, 0)
+            U.check(got[name], value, bound, what + " " + name)
