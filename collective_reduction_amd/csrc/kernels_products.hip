@@ -1345,8 +1345,9 @@ hipError_t matmul(const ProductCall& c) {
   const uint32_t rows = c.capacity / c.per_rank;
   // The form for few rows: up to one pass of 16 rows over the weights per expert
   // on average, where its workgroups (64 columns of an expert each) are no more
-  // than the compute units, and of float32 with rows on the 16-byte grid also
-  // where there are more.  Measured (us, tiles / few rows; weights from memory
+  // than the compute units; of float32 with rows on the 16-byte grid also where
+  // they are no more than twice that, or hidden is at most 2048, so that the
+  // tiles have few stages.  Measured (us, tiles / few rows; weights from memory
   // and, in brackets, from the caches):
   //   workgroups, bf16, 8 rows an expert: 64 (2048 -> 4096) 30 / 15 [17 / 13],
   //     128 19 / 10 [13 / 10], 256 (2048 -> 2048) 32 / 18 [23 / 17], 256 (5120 ->
@@ -1355,14 +1356,16 @@ hipError_t matmul(const ProductCall& c) {
   //     of odd widths 65 (4097 -> 4097) 68 / 64 [52 / 64], 256 40 / 30 [31 / 29],
   //     512 49 / 54; in between it is by the shape: 2048 -> 4096 with 2,048 127 /
   //     120, 32 rows over those 32 experts at random 77 / 70
-  //   float32: 256 58 / 32 [49 / 31], 512 82 / 66, 1,024 87 / 70, 4,096 289 / 254;
-  //     of odd widths 256 66 / 42, 512 91 / 88, 1,024 85 / 93
+  //   float32: 256 58 / 32 [49 / 31], 512 82 / 66 (8192 -> 4096 286 / 247), 1,024
+  //     87 / 70, 4,096 289 / 254; 4096 -> 2048 with 1,024 274 / 278, 5120 -> 2560
+  //     with 1,280 412 / 453; of odd widths 256 66 / 42, 512 91 / 88, 1,024 85 / 93
   //   rows an expert, 256 workgroups, bf16: 16 32 / 19 [23 / 18], 32 32 / 34 [23 / 33];
   //     float32: 16 58 / 33 [49 / 33], 32 58 / 64 [49 / 64]
   const uint32_t columns = (a.n + kWaveN - 1) / kWaveN;
-  const bool narrow = uint64_t(a.nranks) * a.per_rank * columns <= uint64_t(c.num_cus);
-  const bool wide = sizeof(S) == 4 && c.rows16 && c.weights16 && c.hidden * sizeof(S) % 16 == 0;
-  if (rows <= kFewRows && (narrow || wide)) {
+  const uint64_t blocks = uint64_t(a.nranks) * a.per_rank * columns, cus = uint64_t(c.num_cus);
+  const bool wide = sizeof(S) == 4 && c.rows16 && c.weights16 && c.hidden * sizeof(S) % 16 == 0 &&
+                    (blocks <= 2 * cus || c.hidden <= 2048);
+  if (rows <= kFewRows && (blocks <= cus || wide)) {
     // An expert may still have more: those are left to the tiles, in a second
     // launch where the capacity allows for any (2.5 us when there are none).
     if (c.capacity > kFewRows && c.has_offsets) a.least = kFewRows + 1;

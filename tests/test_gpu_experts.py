@@ -466,6 +466,8 @@ def test_few_rows_on_average_and_many_of_one_expert(cs, dtype, rows):
     ("bfloat16", 2, 2, 32, 200, 4096, (16, 16), ("few", "tiles")), ("bfloat16", 2, 2, 32, 200, 4097, (15, 17), ("tiles",)),
     ("bfloat16", 2, 2, 33, 131, 4095, (1, 32), ("few", "tiles")), ("float32", 2, 2, 32, 72, 4097, (17, 15), ("few", "tiles")),
     ("float32", 2, 2, 32, 73, 4097, (9, 16), ("tiles",)), ("float32", 2, 2, 32, 73, 4095, (9, 16), ("few", "tiles")),
+    # float32 on the vector grid: past twice the compute units a long hidden takes the tiles
+    ("float32", 2, 2, 32, 2052, 8193, (9, 16), ("tiles",)), ("float32", 2, 2, 32, 2052, 4097, (9, 16), ("few", "tiles")),
     # no room for more than 16, with offsets and without; one row over
     ("bfloat16", 3, 1, 16, 136, 72, (16,), ("few",)), ("float32", 3, 1, 16, 136, 72, None, ("few",)),
     ("bfloat16", 3, 1, 16, 4104, 72, None, ("few",)), ("bfloat16", 3, 1, 17, 136, 72, None, ("tiles",)),
